@@ -81,8 +81,7 @@ def draw(rng):
         sigmoid = rng.random() < 0.5
         return _route(_log_int(rng, 1, 16384 * 256 // max(E, 256)), E, topk, "sigmoid" if sigmoid else "softmax",
                       groups, topk_groups, 2 if sigmoid else 1, bias=sigmoid and rng.random() < 0.7,
-                      # one choice renormalised weighs the same whatever its score
-                      renorm=topk > 1 and rng.random() < 0.7, scale=rng.choice((1.0, 2.5)), bf16=rng.random() < 0.5,
+                      renorm=rng.random() < 0.7, scale=rng.choice((1.0, 2.5)), bf16=rng.random() < 0.5,
                       train=rng.random() < 0.5)
     H = BLOCK * rng.randint(2, 56)
     if op in ("dispatch", "combine"):
@@ -132,7 +131,7 @@ def work(case):
         back = (T * H * 2 + rows * H * 2 + T * k * 4) if case["train"] else 0
         return {"bytes": read + T * H * 2 + back, "flops": (5 if case["train"] else 2) * rows * H}
     N, K, size = case["N"], case["K"], 2 if case["bf16"] else 4
-    out = case["G"] * N * K * 2
+    out = case["G"] * N * K * 4
     return {"bytes": rows * N * size + T * K * size + out * (2 if case["accumulate"] else 1),
             "flops": 2 * rows * N * K}
 
@@ -200,10 +199,7 @@ def prepare(case, seed):
         dy[row_pair < 0] = 0  # as the gradient of the combine leaves its padding rows
         state["dy"] = dy.to(state["x"].dtype)
     state["longest"] = -(-int(counts.max()) // BLOCK) * BLOCK
-    # gradients in the type of the weights that they are for
-    state["dw"] = None
-    if case["accumulate"]:
-        state["dw"] = torch.randn((G, N, K), generator=gen, device="cuda", dtype=torch.bfloat16).mul_(0.02)
+    state["dw"] = torch.randn((G, N, K), generator=gen, device="cuda") * 0.05 if case["accumulate"] else None
     return state
 
 
@@ -345,7 +341,7 @@ def _plain_wgrad(state):
     past = (at >= last[:, None])[..., None]
     at = at.clamp(max=a.shape[0] - 1)
     dw = torch.matmul(a[at].masked_fill(past, 0).transpose(1, 2).contiguous(), b[at].masked_fill(past, 0))
-    return {"dw": (dw if state["dw"] is None else state["dw"].float() + dw).to(torch.bfloat16)}
+    return {"dw": dw if state["dw"] is None else state["dw"] + dw}
 
 
 # ---- one pass ----------------------------------------------------------------------------------
