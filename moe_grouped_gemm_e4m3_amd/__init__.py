@@ -601,11 +601,11 @@ def grouped_gemm_wgrad_workspace(G: int, M_total: int, N: int, K: int) -> int:
 
 
 def grouped_gemm_wgrad(a, sfa, b, sfb, offsets: torch.Tensor | None = None, c: torch.Tensor | None = None,
-                       d: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16, ue8m0: bool = False,
+                       d: torch.Tensor | None = None, dtype: torch.dtype = torch.float32, ue8m0: bool = False,
                        workspace: torch.Tensor | None = None):
     """a [N,M_total], sfa [M_total/128,N], b [K,M_total], sfb [M_total/128,K] (cast_fp8_per_channel of the output
-    gradient and of the input), offsets [G+1] int32 (None: one group) -> d [G,N,K] bf16 or fp32 (`dtype`, or the
-    type of c or d), plus c [G,N,K] if given (c may be d). workspace: uint8, of at least
+    gradient and of the input), offsets [G+1] int32 (None: one group) -> d [G,N,K] fp32, or bf16 where `dtype`, c
+    or d says so, plus c [G,N,K] if given (c may be d). workspace: uint8, of at least
     grouped_gemm_wgrad_workspace bytes (default: a new one where there is use for it)."""
     _operands(a, sfa, b, sfb)
     if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
