@@ -131,10 +131,11 @@ __device__ __forceinline__ uint32_t quant4_hw(const float v[4], float s) {
 // The quotient v / s correctly rounded, from r = RN(1 / s) by one correction step: q0 = RN(v r), the
 // remainder v - s q0 is exact in an FMA, and q0 plus the remainder times r rounds to v / s unless the
 // remainder underflows, which takes s < 2^-80, or s is not finite. Three operations where a division
-// takes about ten.
+// takes about ten. The remainder is taken as s q0 - v and subtracted: where it vanishes that adds -0, and the
+// quotient -0 stays -0.
 __device__ __forceinline__ float divide_by(float v, float s, float r) {
   const float q0 = v * r;
-  return fmaf(fmaf(-q0, s, v), r, q0);
+  return fmaf(-fmaf(q0, s, -v), r, q0);
 }
 
 // v / s may be taken from RN(1 / s): by divide_by, or (power-of-two scales) as the exact product. Not
