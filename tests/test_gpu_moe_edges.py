@@ -56,3 +56,47 @@ def test_negative_zeros_keep_their_sign(dg, ue8m0, bf16, neighbour):
     q, sf = dg.cast_fp8_per_channel(_device(y, bf16), ue8m0=ue8m0)
     assert_same_bytes(q, qy, "per channel")
     assert_same_bits(sf, np.ascontiguousarray(sy.T), "per channel")
+
+
+# ---- sigmoid gradients at the ends of the range --------------------------------------------
+def _sigmoid_backward(x, ids, g, renormalise, scale):
+    """-> (dlogits, the sizes of the terms of each element), 64 bits; 1 - s as the sigmoid of -x."""
+    x = x.astype(np.float64)
+    with np.errstate(over="ignore"):
+        s, rest = 1.0 / (1.0 + np.exp(-x)), 1.0 / (1.0 + np.exp(x))
+    g = g.astype(np.float64) * scale
+    top = np.take_along_axis(s, ids, 1)
+    size = np.abs(g) * top
+    own = g * top
+    if renormalise:
+        r = top / top.sum(axis=1, keepdims=True)
+        size = (np.abs(g) + (np.abs(g) * r).sum(axis=1, keepdims=True)) * r
+        own = (g - (g * r).sum(axis=1, keepdims=True)) * r
+    rest = np.take_along_axis(rest, ids, 1)
+    want, bound = np.zeros_like(x), np.zeros_like(x)
+    np.put_along_axis(want, ids, own * rest, 1)
+    np.put_along_axis(bound, ids, size * rest, 1)
+    return want, bound
+
+
+def _sigmoid_case(dg, x, ids, g, renormalise, scale, bf16):
+    dx = dg.moe_route_backward(_device(x, bf16), to_dev(ids), to_dev(g), dg.SCORES_SIGMOID, renormalise=renormalise,
+                               scale=scale).float().cpu().numpy().astype(np.float64)
+    want, bound = _sigmoid_backward(x, ids, g, renormalise, scale)
+    # the exponential (2 units), the sum and the quotient of each of two sigmoids, the sums over the choices and the
+    # products between them: some topk + 16 roundings, each of the terms' sizes; subnormal numbers have a step of 2^-149
+    topk = ids.shape[1]
+    tol = 2 * (topk + 16) * U32 * bound + 2.0 ** -148 * (1 + np.abs(g).max() * scale) + (UBF * np.abs(want) if bf16 else 0)
+    assert np.isfinite(dx).all()
+    assert (np.abs(dx - want) <= tol).all(), float((np.abs(dx - want) / np.maximum(tol, 1e-300)).max())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_sigmoid_gradient_of_confident_scores(dg, renormalise, bf16):
+    say("sigmoid gradient renormalise=%s bf16=%s" % (renormalise, bf16))
+    rng = np.random.default_rng(4)
+    x = rng.choice(np.array([10, 12, 16, 17, 20, 30, 60, 80, 1, -1, -10, -30, -60], np.float32), (40, 64))
+    ids = np.argsort(rng.random((40, 64)), axis=1)[:, :6].astype(np.int32)
+    g = rng.standard_normal((40, 6)).astype(np.float32)
+    _sigmoid_case(dg, x, ids, g, renormalise, 2.5, bf16)
