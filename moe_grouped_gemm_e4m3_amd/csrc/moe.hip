@@ -453,11 +453,18 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p) {
     if (p.renormalise) {
       float S = 0.0f, gs = 0.0f;
 #pragma unroll
-      for (int q = 0; q < PICKS; ++q) {
-        S += s[q];
-        gs += g[q] * s[q];
-      }
+      for (int q = 0; q < PICKS; ++q) S += s[q];
       S = seg_sum<L>(S);
+      if (p.sigmoid) {
+        // S may be 1e-38, and 1 / S or a product past fp32: only ratios of scores count, so all of them times
+        // the power of two that brings S to [1/2, 1), which is exact
+        const int up = -__builtin_amdgcn_frexp_expf(S);
+        S = ldexpf(S, up);
+#pragma unroll
+        for (int q = 0; q < PICKS; ++q) s[q] = ldexpf(s[q], up);
+      }
+#pragma unroll
+      for (int q = 0; q < PICKS; ++q) gs += g[q] * s[q];
       gs = seg_sum<L>(gs);
 #pragma unroll
       for (int q = 0; q < PICKS; ++q) g[q] = S == 0.0f || id[q] < 0 ? 0.0f : (g[q] - gs / S) / S;

@@ -100,3 +100,26 @@ def test_sigmoid_gradient_of_confident_scores(dg, renormalise, bf16):
     ids = np.argsort(rng.random((40, 64)), axis=1)[:, :6].astype(np.int32)
     g = rng.standard_normal((40, 6)).astype(np.float32)
     _sigmoid_case(dg, x, ids, g, renormalise, 2.5, bf16)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_sigmoid_gradient_of_vanishing_scores(dg, bf16):
+    # renormalised weights do not vanish with the scores: s of 1e-37 and less, their sum's reciprocal past fp32
+    say("sigmoid gradient of vanishing scores bf16=%s" % bf16)
+    rng = np.random.default_rng(5)
+    x = rng.choice(np.array([-84, -86, -87, -88], np.float32), (40, 64))
+    x[:5] = -88
+    ids = np.argsort(rng.random((40, 64)), axis=1)[:, :6].astype(np.int32)
+    g = (rng.standard_normal((40, 6)) * 100).astype(np.float32)
+    x64 = x.astype(np.float64)
+    s = 1.0 / (1.0 + np.exp(-x64))
+    r = np.take_along_axis(s, ids, 1)
+    steps = 2.0 ** -149 / r.min()               # what a subnormal score is good for
+    assert steps < 2.0 ** -21
+    dx = dg.moe_route_backward(_device(x, bf16), to_dev(ids), to_dev(g), dg.SCORES_SIGMOID, scale=2.5)
+    dx = dx.float().cpu().numpy().astype(np.float64)
+    want, bound = _sigmoid_backward(x, ids, g, True, 2.5)
+    # a score, its share of the sum and the sum over the shares each carry that step
+    tol = (4 * steps + 2 * (6 + 16) * U32) * bound + (UBF * np.abs(want) if bf16 else 0)
+    assert np.isfinite(dx).all()
+    assert (np.abs(dx - want) <= tol).all()
