@@ -456,9 +456,9 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p) {
       for (int q = 0; q < PICKS; ++q) S += s[q];
       S = seg_sum<L>(S);
       if (p.sigmoid) {
-        // S may be 1e-38, and 1 / S or a product past fp32: only ratios of scores count, so all of them times
-        // the power of two that brings S to [1/2, 1), which is exact
-        const int up = -__builtin_amdgcn_frexp_expf(S);
+        // S may be 1e-38, and 1 / S or a product past fp32: only ratios of scores count, so a smaller S and all
+        // of them times the power of two that brings it to [1/2, 1), which is exact
+        const int up = max(-__builtin_amdgcn_frexp_expf(S), 0);
         S = ldexpf(S, up);
 #pragma unroll
         for (int q = 0; q < PICKS; ++q) s[q] = ldexpf(s[q], up);
