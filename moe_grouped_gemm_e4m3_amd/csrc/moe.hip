@@ -158,6 +158,17 @@ __device__ __forceinline__ void softmax_sums(const float (&x)[NPER], int E, floa
 }
 __device__ __forceinline__ float softmax_at(float x, float mx, float sum) { return sum == 0.0f ? 0.0f : expf(x - mx) / sum; }
 
+// A row whose softmax is NaN: one that holds a NaN or +infinity.
+template <int L, int NPER>
+__device__ __forceinline__ bool row_is_nan(const float (&x)[NPER]) {
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) found = found || !(x[i] < INFINITY);
+  uint64_t any = __ballot(found);
+  if (L == 32) any = (threadIdx.x & 32) ? any >> 32 : any & 0xFFFFFFFFu;
+  return any != 0;
+}
+
 // A wave's LDS operations run in order; this keeps the compiler from moving others across, and waits.
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
@@ -371,7 +382,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem p) {
       total += w[q];
     }
   } else {
-    // the softmax's own sum cancels: e^x over the chosen alone, without its underflow
+    // the softmax's own sum cancels: e^x over the chosen alone, without its underflow. A NaN or +infinity
+    // anywhere in the row makes that sum NaN, and so the weights
     float top = -INFINITY;
 #pragma unroll
     for (int q = 0; q < PICKS; ++q) {
@@ -380,14 +392,10 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem p) {
     }
     top = seg_max<L>(top);
     if (top == -INFINITY) top = 0.0f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) nan = nan || x[i] != x[i];
-    uint64_t any = __ballot(nan);
-    if (L == 32) any = (threadIdx.x & 32) ? any >> 32 : any & 0xFFFFFFFFu;
+    const bool nan = row_is_nan<L, NPER>(x);
 #pragma unroll
     for (int q = 0; q < PICKS; ++q) {
-      w[q] = sl + q * L < p.topk ? (any != 0 ? NAN : expf(w[q] - top)) : 0.0f;
+      w[q] = sl + q * L < p.topk ? (nan ? NAN : expf(w[q] - top)) : 0.0f;
       total += w[q];
     }
   }

@@ -123,3 +123,22 @@ def test_sigmoid_gradient_of_vanishing_scores(dg, bf16):
     tol = (4 * steps + 2 * (6 + 16) * U32) * bound + (UBF * np.abs(want) if bf16 else 0)
     assert np.isfinite(dx).all()
     assert (np.abs(dx - want) <= tol).all()
+
+
+# ---- infinities and NaN among the logits ---------------------------------------------------
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("how", [dict(), dict(bias=True), dict(groups=10, topk_groups=3, group_top=2),
+                                 dict(bias=True, groups=2, topk_groups=1)], ids=str)
+def test_softmax_rows_with_an_infinity_weigh_nan(dg, how, renormalise):
+    how, E = dict(how), 130
+    x = np.random.default_rng(7).standard_normal((7, E)).astype(np.float32)
+    x[1, 100] = x[2, 0] = x[5, 129] = np.inf
+    x[3, 64] = np.nan
+    if how.pop("bias", False):
+        how["bias"] = to_dev(np.linspace(0.01, 0.0, E).astype(np.float32))
+    for bf16 in (False, True):
+        ids, w = dg.moe_route(_device(x, bf16), 5, dg.SCORES_SOFTMAX, renormalise=renormalise, **how)
+        ids, w = ids.cpu().numpy(), w.cpu().numpy()
+        assert (ids >= 0).all() and (ids < E).all() and all(len(set(r)) == 5 for r in ids.tolist())
+        assert np.isnan(w[[1, 2, 3, 5]]).all()
+        assert np.isfinite(w[[0, 4, 6]]).all()
