@@ -309,7 +309,9 @@ dg_status_t dg_moe_route(const void* logits, dg_input_dtype_t dtype, int64_t T, 
  * dweights [T,topk] fp32. The choice itself has no gradient, and neither has the bias. With S
  * the sum of s over the chosen: ds_i = scale * dw_i, renormalised scale / S * (dw_i -
  * sum_j dw_j s_j / S) (0 where S = 0); sigmoid dx = ds s (1 - s); softmax dx_j = s_j (ds_j -
- * sum_i ds_i s_i). An id outside [0,E) contributes nothing.
+ * sum_i ds_i s_i). An id outside [0,E) contributes nothing. Where dg_moe_route's weights are NaN the
+ * gradient is: softmax, a NaN or +infinity in the row makes all of it NaN; sigmoid, a NaN that was
+ * chosen its own element and, renormalised, the other chosen ones'.
  */
 dg_status_t dg_moe_route_backward(const void* logits, dg_input_dtype_t dtype, int64_t T, int32_t E, int32_t scores,
                                   int32_t topk, int32_t renormalise, float scale, const int32_t* ids,

@@ -418,8 +418,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem p) {
 // else ds_i = scale g_i. Sigmoid: dx = ds s (1 - s) on C, 0 elsewhere, 1 - s as the sigmoid of -x (the
 // difference is 6 % off at x = 16 and 0 from 17 on); softmax:
 // dx_j = s_j (ds_j - sum_C ds_i s_i). Renormalised, that last sum is 0 and s_i ds_i depends on
-// s_i / S alone, so the chosen logits are all that is read: the whole row only for a softmax
-// that is not renormalised. The chosen experts' parts reach the lanes that write them through LDS.
+// s_i / S alone: of a softmax row the rest is then read only for a NaN or +infinity, which makes the whole
+// row's scores, weights and gradient NaN. Of a sigmoid row the chosen logits are all that is read. The chosen experts' parts reach the lanes that write them through LDS.
 // 16384 tokens x 256 experts: 8.7 us, 17 MB written; bound by the chain of the ids, the logits that they
 // name, and the row, more than by HBM. 5001 x 160 softmax, not renormalised: 4.5 us.
 template <bool kBf16, int L, int NPER>
@@ -433,6 +433,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p) {
   const int64_t tt = live ? t : p.T - 1;
   const int E = p.E;
   float* mine = row[threadIdx.x / L];
+  float x[NPER];
+  if (!p.sigmoid) load_row<kBf16, L, NPER>(p.logits, tt, E, x);
   constexpr int PICKS = 64 / L;
   int id[PICKS];
   float xj[PICKS], g[PICKS], s[PICKS], own[PICKS];
@@ -479,11 +481,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p) {
     }
 #pragma unroll
     for (int q = 0; q < PICKS; ++q) own[q] = p.sigmoid ? g[q] * s[q] * sigmoid(-xj[q]) : g[q] * s[q];
+    const float rest = !p.sigmoid && row_is_nan<L, NPER>(x) ? NAN : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) dx[i] = 0.0f;
+    for (int i = 0; i < NPER; ++i) dx[i] = rest;
   } else {
-    float x[NPER], mx, sum;
-    load_row<kBf16, L, NPER>(p.logits, tt, E, x);
+    float mx, sum;
     softmax_sums<L, NPER>(x, E, mx, sum);
     float inner = 0.0f;
 #pragma unroll

@@ -142,3 +142,20 @@ def test_softmax_rows_with_an_infinity_weigh_nan(dg, how, renormalise):
         assert (ids >= 0).all() and (ids < E).all() and all(len(set(r)) == 5 for r in ids.tolist())
         assert np.isnan(w[[1, 2, 3, 5]]).all()
         assert np.isfinite(w[[0, 4, 6]]).all()
+
+
+@pytest.mark.parametrize("T,E", [(6, 130), (5, 256), (7, 600)])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_softmax_gradient_of_rows_whose_weights_are_nan(dg, bf16, renormalise, T, E):
+    # the weights of such a row are NaN, whichever expert brought it, and so is their gradient
+    say("softmax gradient of NaN rows E=%d renormalise=%s bf16=%s" % (E, renormalise, bf16))
+    x = np.random.default_rng(8).standard_normal((T, E)).astype(np.float32)
+    x[1, E - 1], x[2, 3], x[3, E // 2] = np.nan, np.inf, -np.inf
+    ids = np.tile(np.array([5, 9, 11], np.int32), (T, 1))  # none of those
+    g = np.random.default_rng(9).standard_normal((T, 3)).astype(np.float32)
+    dx = dg.moe_route_backward(_device(x, bf16), to_dev(ids), to_dev(g), dg.SCORES_SOFTMAX, renormalise=renormalise)
+    dx = dx.float().cpu().numpy()
+    assert np.isnan(dx[[1, 2]]).all()
+    keep = [t for t in range(T) if t not in (1, 2)]
+    assert np.isfinite(dx[keep]).all() and (dx[keep][:, [5, 9, 11]] != 0).any()
