@@ -54,6 +54,20 @@ hipError_t launch_cast_per_block(const void* w, int bf16, int pow2, int64_t N, i
 // Compute units of the current device (cached per device; 256 on MI355X).
 int cu_count();
 
+// A launch holds fewer than 2^32 threads: workgroups of 256 past that go to further launches, each told
+// the number of its first. Every piece but the last is a multiple of the 8 XCDs, so that a workgroup's
+// number says which XCD it runs on as in one launch.
+constexpr int64_t kPieceWorkgroups = (1 << 24) - 8;
+template <typename Launch>
+hipError_t launch_in_pieces(int64_t wgs, Launch launch) {
+  for (int64_t wg0 = 0; wg0 < wgs; wg0 += kPieceWorkgroups) {
+    launch(dim3((unsigned)(wgs - wg0 < kPieceWorkgroups ? wgs - wg0 : kPieceWorkgroups)), wg0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // ---- mixture-of-experts operators (moe.hip) ----
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 64;

@@ -272,12 +272,12 @@ __device__ __forceinline__ void sort_run(uint32_t (&k)[N], uint64_t& order) {
 // holder, 16.4 with that alone); 5001 x 160 softmax: 5.9 us (10.2 with powers of two only as runs); one
 // token: 4.8 us.
 template <bool kBf16, int L, int NPER>
-__global__ __launch_bounds__(256) void route_kernel(RouteProblem p) {
+__global__ __launch_bounds__(256) void route_kernel(RouteProblem p, int64_t wg0) {
   extern __shared__ uint32_t lds[];
   __shared__ int picks[256 / L][kMaxTopk];
   const int sl = seg_lane<L>(), e0 = sl * NPER;
-  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int64_t wave_t = (int64_t)blockIdx.x * (256 / L) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * (64 / L);
+  const int64_t t = (wg0 + blockIdx.x) * (256 / L) + threadIdx.x / L;
+  const int64_t wave_t = (wg0 + blockIdx.x) * (256 / L) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * (64 / L);
   if (wave_t >= p.T) return;
   const bool live = t < p.T;  // the second token of the last wave may not be there: it repeats the last one
   const int64_t tt = live ? t : p.T - 1;
@@ -423,11 +423,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem p) {
 // 16384 tokens x 256 experts: 8.7 us, 17 MB written; bound by the chain of the ids, the logits that they
 // name, and the row, more than by HBM. 5001 x 160 softmax, not renormalised: 4.5 us.
 template <bool kBf16, int L, int NPER>
-__global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p) {
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p, int64_t wg0) {
   __shared__ __attribute__((aligned(16))) float row[256 / L][L * NPER];
   const int sl = seg_lane<L>(), e0 = sl * NPER;
-  const int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int64_t wave_t = (int64_t)blockIdx.x * (256 / L) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * (64 / L);
+  const int64_t t = (wg0 + blockIdx.x) * (256 / L) + threadIdx.x / L;
+  const int64_t wave_t = (wg0 + blockIdx.x) * (256 / L) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * (64 / L);
   if (wave_t >= p.T) return;
   const bool live = t < p.T;
   const int64_t tt = live ? t : p.T - 1;
@@ -811,12 +811,13 @@ __global__ __launch_bounds__(256) void layout_place_kernel(LayoutProblem p, int 
 // The workgroups past the tokens (contiguous layout) write zero codes and scales into the rows
 // without a token of one block in use each, which the GEMM reads.
 template <bool kBf16, bool kPow2, bool kStream>
-__global__ __launch_bounds__(256) void dispatch_kernel(DispatchProblem p, uint32_t token_wgs) {
+__global__ __launch_bounds__(256) void dispatch_kernel(DispatchProblem p, uint32_t token_wgs, int64_t wg0) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t nseg = (uint32_t)(p.kblocks + 7) / 8;
   const int64_t H = (int64_t)p.kblocks * kQ;
-  if (blockIdx.x < token_wgs) {
-    const uint32_t u = xcd_remap(blockIdx.x, token_wgs) * 4 + (uint32_t)w;
+  const uint32_t wg = (uint32_t)wg0 + blockIdx.x;
+  if (wg < token_wgs) {
+    const uint32_t u = xcd_remap(wg, token_wgs) * 4 + (uint32_t)w;
     const uint32_t t = u / nseg, seg = u - t * nseg;
     if (t >= p.T) return;
     const int kb = (int)seg * 8 + (lane >> 3);  // this lane's K block
@@ -847,7 +848,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(DispatchProblem p, uint32
     }
     return;
   }
-  const int64_t block = blockIdx.x - token_wgs, r0 = block * kQ + w * 32;
+  const int64_t block = wg - token_wgs, r0 = block * kQ + w * 32;
   if (p.row_pair[block * kQ] < 0) return;  // not in use
   uint64_t empty = __ballot(lane < 32 && p.row_pair[r0 + (lane & 31)] < 0);
   while (empty != 0) {
@@ -882,9 +883,9 @@ __device__ __forceinline__ v4i pack8(const float (&v)[8]) {
 // out[t] = sum_j w[t,j] y[pos[t,j]], summed in fp32 in the order of the choices and rounded once.
 // One wave per token and 512 columns.
 template <bool kStream>
-__global__ __launch_bounds__(256) void combine_kernel(CombineProblem p) {
+__global__ __launch_bounds__(256) void combine_kernel(CombineProblem p, int64_t wg0) {
   const int lane = threadIdx.x & 63;
-  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t u = (wg0 + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int64_t nseg = (p.H + 511) / 512;
   if (u >= p.T * nseg) return;
   const int64_t t = u / nseg, col = (u - t * nseg) * 512 + lane * 8;
@@ -906,13 +907,13 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineProblem p) {
 // workgroups past the pairs (contiguous layout, row_pair given) write zeros into the rows without a
 // token of the used blocks.
 template <bool kStream>
-__global__ __launch_bounds__(256) void combine_backward_kernel(CombineProblem p) {
+__global__ __launch_bounds__(256) void combine_backward_kernel(CombineProblem p, int64_t wg0) {
   const int lane = threadIdx.x & 63;
   const int64_t pairs = p.T * p.topk;
   const int64_t pair_wgs = (pairs + 3) / 4;
-  const int64_t H = p.H;
-  if ((int64_t)blockIdx.x < pair_wgs) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t H = p.H, wg = wg0 + blockIdx.x;
+  if (wg < pair_wgs) {
+    const int64_t i = wg * 4 + (threadIdx.x >> 6);
     if (i >= pairs) return;
     const int64_t r = p.pos[i], t = i / p.topk;
     if (r < 0 || r >= p.rows) {
@@ -936,12 +937,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineProblem p)
     if (lane == 0) p.dweights[i] = dot;
     return;
   }
-  const int64_t r = ((int64_t)blockIdx.x - pair_wgs) * 4 + (threadIdx.x >> 6);
+  const int64_t r = (wg - pair_wgs) * 4 + (threadIdx.x >> 6);
   if (r >= p.rows || p.row_pair[r] >= 0 || p.row_pair[r & ~(int64_t)(kQ - 1)] < 0) return;
   for (int64_t col = lane * 8; col < H; col += 512) *reinterpret_cast<v4i*>(p.dy + r * H + col) = v4i{0, 0, 0, 0};
 }
-
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 
 }  // namespace
 
@@ -955,13 +954,13 @@ hipError_t launch_route(const RouteProblem& p, hipStream_t stream) {
 #define DG_X(l, n)                                                                                               \
   if (p.E <= l * n) {                                                                                            \
     const int64_t wgs = (p.T + 256 / l - 1) / (256 / l);                                                         \
-    if (wgs > kMaxGrid) return hipErrorInvalidValue;                                                             \
     const int per = p.E / p.groups, run = per / n;                                                               \
     const bool in_lds = p.groups > 1 && (per % n != 0 || (run & (run - 1)) != 0);                                \
     const size_t bytes = in_lds ? (size_t)(256 / l) * (p.E + 64) * 4 : 0;                                        \
-    if (p.bf16) route_kernel<true, l, n><<<dim3((unsigned)wgs), dim3(256), bytes, stream>>>(p);                  \
-    else route_kernel<false, l, n><<<dim3((unsigned)wgs), dim3(256), bytes, stream>>>(p);                        \
-    return hipGetLastError();                                                                                    \
+    return launch_in_pieces(wgs, [&](dim3 grid, int64_t wg0) {                                                   \
+      if (p.bf16) route_kernel<true, l, n><<<grid, dim3(256), bytes, stream>>>(p, wg0);                          \
+      else route_kernel<false, l, n><<<grid, dim3(256), bytes, stream>>>(p, wg0);                                \
+    });                                                                                                          \
   }
   DG_ROUTE_CONFIGS(DG_X)
 #undef DG_X
@@ -971,11 +970,10 @@ hipError_t launch_route(const RouteProblem& p, hipStream_t stream) {
 hipError_t launch_route_backward(const RouteProblem& p, hipStream_t stream) {
 #define DG_X(l, n)                                                                                               \
   if (p.E <= l * n) {                                                                                            \
-    const int64_t wgs = (p.T + 256 / l - 1) / (256 / l);                                                         \
-    if (wgs > kMaxGrid) return hipErrorInvalidValue;                                                             \
-    if (p.bf16) route_backward_kernel<true, l, n><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);             \
-    else route_backward_kernel<false, l, n><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);                   \
-    return hipGetLastError();                                                                                    \
+    return launch_in_pieces((p.T + 256 / l - 1) / (256 / l), [&](dim3 grid, int64_t wg0) {                       \
+      if (p.bf16) route_backward_kernel<true, l, n><<<grid, dim3(256), 0, stream>>>(p, wg0);                     \
+      else route_backward_kernel<false, l, n><<<grid, dim3(256), 0, stream>>>(p, wg0);                           \
+    });                                                                                                          \
   }
   DG_ROUTE_CONFIGS(DG_X)
 #undef DG_X
@@ -998,22 +996,23 @@ hipError_t launch_layout(const LayoutProblem& p, hipStream_t stream) {
 hipError_t launch_dispatch(const DispatchProblem& p, int bf16, int pow2, hipStream_t stream) {
   const int64_t token_wgs = (p.T * ((p.kblocks + 7) / 8) + 3) / 4;
   const int64_t wgs = token_wgs + (p.masked ? 0 : p.rows / kQ);
-  if (wgs > kMaxGrid / 4) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs), block(256);
+  if (wgs > 0x1FFFFFFF) return hipErrorInvalidValue;  // 2^31 waves: terabytes of tokens
   const uint32_t n = (uint32_t)token_wgs;
   // more codes than the chip's L2s (32 MB) hold
   const bool past = p.T * p.topk * p.kblocks * kQ > (int64_t)32 << 20;
-  switch ((bf16 ? 4 : 0) + (pow2 ? 2 : 0) + (past ? 1 : 0)) {
-    case 0: dispatch_kernel<false, false, false><<<grid, block, 0, stream>>>(p, n); break;
-    case 1: dispatch_kernel<false, false, true><<<grid, block, 0, stream>>>(p, n); break;
-    case 2: dispatch_kernel<false, true, false><<<grid, block, 0, stream>>>(p, n); break;
-    case 3: dispatch_kernel<false, true, true><<<grid, block, 0, stream>>>(p, n); break;
-    case 4: dispatch_kernel<true, false, false><<<grid, block, 0, stream>>>(p, n); break;
-    case 5: dispatch_kernel<true, false, true><<<grid, block, 0, stream>>>(p, n); break;
-    case 6: dispatch_kernel<true, true, false><<<grid, block, 0, stream>>>(p, n); break;
-    default: dispatch_kernel<true, true, true><<<grid, block, 0, stream>>>(p, n); break;
-  }
-  return hipGetLastError();
+  return launch_in_pieces(wgs, [&](dim3 grid, int64_t wg0) {
+    const dim3 block(256);
+    switch ((bf16 ? 4 : 0) + (pow2 ? 2 : 0) + (past ? 1 : 0)) {
+      case 0: dispatch_kernel<false, false, false><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 1: dispatch_kernel<false, false, true><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 2: dispatch_kernel<false, true, false><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 3: dispatch_kernel<false, true, true><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 4: dispatch_kernel<true, false, false><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 5: dispatch_kernel<true, false, true><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      case 6: dispatch_kernel<true, true, false><<<grid, block, 0, stream>>>(p, n, wg0); break;
+      default: dispatch_kernel<true, true, true><<<grid, block, 0, stream>>>(p, n, wg0); break;
+    }
+  });
 }
 
 // The rows that these pairs can name are more than the 256 MB of the Infinity Cache.
@@ -1023,19 +1022,18 @@ static bool past_caches(const CombineProblem& p) {
 }
 
 hipError_t launch_combine(const CombineProblem& p, hipStream_t stream) {
-  const int64_t wgs = (p.T * ((p.H + 511) / 512) + 3) / 4;
-  if (wgs > kMaxGrid) return hipErrorInvalidValue;
-  if (past_caches(p)) combine_kernel<true><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);
-  else combine_kernel<false><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);
-  return hipGetLastError();
+  return launch_in_pieces((p.T * ((p.H + 511) / 512) + 3) / 4, [&](dim3 grid, int64_t wg0) {
+    if (past_caches(p)) combine_kernel<true><<<grid, dim3(256), 0, stream>>>(p, wg0);
+    else combine_kernel<false><<<grid, dim3(256), 0, stream>>>(p, wg0);
+  });
 }
 
 hipError_t launch_combine_backward(const CombineProblem& p, hipStream_t stream) {
   const int64_t wgs = (p.T * p.topk + 3) / 4 + (p.row_pair ? (p.rows + 3) / 4 : 0);
-  if (wgs > kMaxGrid) return hipErrorInvalidValue;
-  if (past_caches(p)) combine_backward_kernel<true><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);
-  else combine_backward_kernel<false><<<dim3((unsigned)wgs), dim3(256), 0, stream>>>(p);
-  return hipGetLastError();
+  return launch_in_pieces(wgs, [&](dim3 grid, int64_t wg0) {
+    if (past_caches(p)) combine_backward_kernel<true><<<grid, dim3(256), 0, stream>>>(p, wg0);
+    else combine_backward_kernel<false><<<grid, dim3(256), 0, stream>>>(p, wg0);
+  });
 }
 
 }  // namespace dg

@@ -24,12 +24,13 @@ namespace {
 // alone. Bound by HBM: 2 or 4 bytes in, one out per element. 8192 rows of 7168 in bf16: 33 us, 5.4 TB/s;
 // 4001 of 18432: 38 us, 5.8 TB/s.
 template <bool kBf16, bool kPow2>
-__global__ __launch_bounds__(256) void cast_per_channel_kernel(ChannelCastProblem p) {
+__global__ __launch_bounds__(256) void cast_per_channel_kernel(ChannelCastProblem p, int64_t wg0) {
   __shared__ __attribute__((aligned(16))) float wave_amax[4][64], scale[64], reciprocal[64];
   __shared__ __attribute__((aligned(16))) uint8_t tile[64 * kQ];
   const uint32_t per_block = (uint32_t)(p.K / 64);  // workgroups per 128 rows
-  const int64_t blk = blockIdx.x / per_block;
-  const int64_t m0 = blk * kQ, k0 = (int64_t)(blockIdx.x % per_block) * 64;
+  const uint32_t wg = (uint32_t)wg0 + blockIdx.x;
+  const int64_t blk = wg / per_block;
+  const int64_t m0 = blk * kQ, k0 = (int64_t)(wg % per_block) * 64;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int c8 = t & 7, r4 = t >> 3;
   int64_t src[4];
@@ -699,13 +700,14 @@ int64_t wgrad_workspace(int64_t G, int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_cast_per_channel(const ChannelCastProblem& p, int bf16, int pow2, hipStream_t stream) {
   const int64_t wgs = (p.K / 64) * (p.M_out / kQ);
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs), block(256);
-  if (bf16 && pow2) cast_per_channel_kernel<true, true><<<grid, block, 0, stream>>>(p);
-  else if (bf16) cast_per_channel_kernel<true, false><<<grid, block, 0, stream>>>(p);
-  else if (pow2) cast_per_channel_kernel<false, true><<<grid, block, 0, stream>>>(p);
-  else cast_per_channel_kernel<false, false><<<grid, block, 0, stream>>>(p);
-  return hipGetLastError();
+  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;  // 16 TB of codes
+  return launch_in_pieces(wgs, [&](dim3 grid, int64_t wg0) {
+    const dim3 block(256);
+    if (bf16 && pow2) cast_per_channel_kernel<true, true><<<grid, block, 0, stream>>>(p, wg0);
+    else if (bf16) cast_per_channel_kernel<true, false><<<grid, block, 0, stream>>>(p, wg0);
+    else if (pow2) cast_per_channel_kernel<false, true><<<grid, block, 0, stream>>>(p, wg0);
+    else cast_per_channel_kernel<false, false><<<grid, block, 0, stream>>>(p, wg0);
+  });
 }
 
 hipError_t launch_wgrad(const WgradProblem& problem, float* workspace, hipStream_t stream, const char** chosen) {

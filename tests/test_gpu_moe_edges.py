@@ -159,3 +159,54 @@ def test_softmax_gradient_of_rows_whose_weights_are_nan(dg, bf16, renormalise, T
     assert np.isnan(dx[[1, 2]]).all()
     keep = [t for t in range(T) if t not in (1, 2)]
     assert np.isfinite(dx[keep]).all() and (dx[keep][:, [5, 9, 11]] != 0).any()
+
+
+# ---- more workgroups than one launch holds -------------------------------------------------
+WORKGROUPS = (1 << 24) + 1  # of 256 threads, 2^32 threads and more
+
+
+def test_routing_more_tokens_than_one_launch_holds(dg):
+    T = WORKGROUPS * 8 - 3                      # 8 tokens to a workgroup
+    say("routing of %d tokens" % T)
+    x = torch.randn((T, 2), device=dev(), dtype=torch.bfloat16)
+    ids, w = dg.moe_route(x, 1, dg.SCORES_SIGMOID, renormalise=False)
+    assert torch.equal(ids[:, 0], (x[:, 1] > x[:, 0]).int())
+    g = torch.randn((T, 1), device=dev())
+    dx = dg.moe_route_backward(x, ids, g, dg.SCORES_SIGMOID, renormalise=False)
+    assert bool((dx.gather(1, 1 - ids.long()) == 0).all())
+    top = x.gather(1, ids.long()).float()
+    assert bool(((w - torch.sigmoid(top)).abs() <= 1e-6).all())
+    assert bool(((dx.gather(1, ids.long()).float() - g * torch.sigmoid(top) * torch.sigmoid(-top)).abs()
+                 <= 2.0 ** -8 * g.abs()).all())
+
+
+def test_moving_more_tokens_than_one_launch_holds(dg):
+    H, rows = 128, 128
+    T = WORKGROUPS * 4 - 1                      # a token to a wave
+    say("moving %d tokens" % T)
+    at = torch.tensor([0, T // 2, ((1 << 24) - 8) * 4 - 1, ((1 << 24) - 8) * 4, T - 2, T - 1], device=dev())
+    n = len(at)
+    pos = torch.full((T, 1), -1, dtype=torch.int32, device=dev())
+    pos[at, 0] = torch.arange(n, dtype=torch.int32, device=dev())
+    w = torch.full((T, 1), 2.0, device=dev())
+    y = torch.randn((rows, H), device=dev()).to(torch.bfloat16)
+    out = torch.full((T, H), 3.0, dtype=torch.bfloat16, device=dev())
+    dg.moe_combine(y, pos, w, out=out)
+    assert torch.equal(out[at], (2.0 * y[:n].float()).to(torch.bfloat16))
+    assert int(torch.stack([out[i:i + (1 << 22)].count_nonzero() for i in range(0, T, 1 << 22)]).sum()) == int(
+        y[:n].count_nonzero())
+    row_pair = torch.full((rows,), -1, dtype=torch.int32, device=dev())
+    row_pair[:n] = at.int()
+    out.copy_(torch.randn((1, H), device=dev()).expand(T, H))
+    out[at] = torch.randn((n, H), device=dev()).to(torch.bfloat16)
+    dy = torch.full((rows, H), 3.0, dtype=torch.bfloat16, device=dev())
+    _, dw = dg.moe_combine_backward(out, y, pos, row_pair, w, dy=dy)
+    assert torch.equal(dy[:n], (2.0 * out[at].float()).to(torch.bfloat16)) and bool((dy[n:] == 0).all())
+    want = (out[at].double() * y[:n].double()).sum(1)
+    assert bool(((dw[at, 0].double() - want).abs() <= 1e-5 * out[at].double().norm(dim=1) * y[:n].double().norm(dim=1)).all())
+    dw[at] = 0
+    assert int(dw.count_nonzero()) == 0
+    q, sf = dg.moe_dispatch_fp8(out, pos, row_pair)
+    want_q, want_s = dg.cast_fp8_per_token(out[at])
+    assert torch.equal(q[:n], want_q) and torch.equal(sf[:, :n], want_s)
+    assert bool((q[n:] == 0).all()) and bool((sf[:, n:] == 0).all())
