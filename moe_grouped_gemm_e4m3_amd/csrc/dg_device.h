@@ -49,9 +49,11 @@ __device__ __forceinline__ uint32_t e4m3_hw_pack4(float y0, float y1, float y2, 
 
 // The smallest power of two >= v (v >= 0), and >= 2^-126, from the fp32 bits: a normal v
 // with a zero mantissa is a power of two already; otherwise the exponent goes up by one.
-// This is the UE8M0 (power-of-two) scale of the casts.
+// This is the UE8M0 (power-of-two) scale of the casts. NaN, the largest value of a chunk of NaN alone, stays
+// NaN, and so do the chunk's codes.
 __device__ __forceinline__ float pow2_ceil(float v) {
   const uint32_t b = __float_as_uint(v);
+  if (b > 0x7F800000u) return v;
   if (b < 0x00800000u) return __uint_as_float(0x00800000u);  // 0 and subnormals
   const uint32_t e = (b >> 23) + ((b & 0x007FFFFFu) ? 1u : 0u);
   return __uint_as_float(e << 23);

@@ -210,3 +210,21 @@ def test_moving_more_tokens_than_one_launch_holds(dg):
     want_q, want_s = dg.cast_fp8_per_token(out[at])
     assert torch.equal(q[:n], want_q) and torch.equal(sf[:, :n], want_s)
     assert bool((q[n:] == 0).all()) and bool((sf[:, n:] == 0).all())
+
+
+def test_chunks_of_nan_alone_stay_nan(dg):
+    # a power-of-two scale of such a chunk is NaN, as its fp32 scale is; it does not turn into zeros
+    say("chunks of NaN alone")
+    x = np.random.default_rng(10).standard_normal((128, 256)).astype(np.float32)
+    x[3, 128:] = np.nan
+    rows = np.random.default_rng(11).standard_normal((128, 256)).astype(np.float32)
+    rows[:, 7] = -np.nan
+    pos, row_pair, _ = dg.moe_layout_masked(torch.zeros((128, 1), dtype=torch.int32, device=dev()), 1, 128)
+    for bf16 in (False, True):
+        for ue8m0 in (False, True):
+            q, sf = (t[0].cpu().numpy() for t in dg.moe_dispatch_fp8(_device(x, bf16), pos, row_pair, ue8m0=ue8m0))
+            assert ((q[3, 128:] & 0x7F) == 0x7F).all() and np.isnan(sf[1, 3])
+            assert np.isfinite(sf).sum() == sf.size - 1 and ((q & 0x7F) == 0x7F).sum() == 128
+            q, sf = (t.cpu().numpy() for t in dg.cast_fp8_per_channel(_device(rows, bf16), ue8m0=ue8m0))
+            assert ((q[7] & 0x7F) == 0x7F).all() and np.isnan(sf[0, 7])
+            assert np.isfinite(sf).sum() == sf.size - 1 and ((q & 0x7F) == 0x7F).sum() == 128
