@@ -268,9 +268,9 @@ __device__ __forceinline__ void sort_run(uint32_t (&k)[N], uint64_t& order) {
 // row's best key is the largest of L first ones: per choice a reduction, and a shift in the first lane that
 // holds it. Bound by the vector ALU (a row of 256 is 1 KB but some 450 instructions, a fifth of them the
 // sigmoids): two tokens to a wave share those of the reductions and the choices. 16384 tokens x 256
-// experts, 8 of 4 of 8 groups: 14.1 us (18.5 with one token to a wave and a second reduction for the
-// holder, 16.4 with that alone); 5001 x 160 softmax: 5.9 us (10.2 with powers of two only as runs); one
-// token: 4.8 us.
+// experts, 8 of 4 of 8 groups: 14.8 us, 13.9 replayed (18.5 with one token to a wave and a second reduction for the
+// holder, 16.4 with that alone); 5001 x 160 softmax: 6.4 us (10.2 with powers of two only as runs); one
+// token: 4.3 us.
 template <bool kBf16, int L, int NPER>
 __global__ __launch_bounds__(256) void route_kernel(RouteProblem p, int64_t wg0) {
   extern __shared__ uint32_t lds[];
@@ -420,8 +420,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem p, int64_t wg0)
 // dx_j = s_j (ds_j - sum_C ds_i s_i). Renormalised, that last sum is 0 and s_i ds_i depends on
 // s_i / S alone: of a softmax row the rest is then read only for a NaN or +infinity, which makes the whole
 // row's scores, weights and gradient NaN. Of a sigmoid row the chosen logits are all that is read. The chosen experts' parts reach the lanes that write them through LDS.
-// 16384 tokens x 256 experts: 8.7 us, 17 MB written; bound by the chain of the ids, the logits that they
-// name, and the row, more than by HBM. 5001 x 160 softmax, not renormalised: 4.5 us.
+// 16384 tokens x 256 experts: sigmoid 8.4 us, 17 MB written, bound by the chain of the ids, the logits that
+// they name, and the row, more than by HBM; softmax 9.1 us renormalised, 10.0 not. 5001 x 160 softmax, not
+// renormalised: 4.9 us.
 template <bool kBf16, int L, int NPER>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p, int64_t wg0) {
   __shared__ __attribute__((aligned(16))) float row[256 / L][L * NPER];
@@ -517,7 +518,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem p, int
 // integer atomics), which gives it its first row, and then places its own pairs in order. Waves take
 // consecutive stretches of the ids, four ids a lane and kLayoutBatch loads in flight; ids that fit
 // one batch per wave (32768 pairs) are read once.
-// 32768 pairs over 32 experts: 11.3 us, bound by the vector ALU (some 150 instructions per 256 ids).
+// 32768 pairs over 32 experts: 11.5 us, bound by the vector ALU (some 150 instructions per 256 ids).
 constexpr int kLayoutThreads = 1024, kLayoutWaves = kLayoutThreads / 64, kLayoutBatch = 8;
 
 // Bits of a wave mask below this lane, added to `more`.
@@ -660,8 +661,9 @@ __device__ __forceinline__ void store16(void* p, v4i v) {
   else *static_cast<v4i*>(p) = v;
 }
 
-// The same sort for many pairs, in three launches over chunks of the ids: 131072 pairs take 18 us over
-// 32 experts and 20 over 256, where every expert's workgroup looking at every id takes 36 and 35. Until
+// The same sort for many pairs, in three launches over chunks of the ids: 131072 pairs take 17 us over
+// 32 experts and 20 over 256, where every expert's workgroup looking at every id takes 36 and 35; 1048576
+// over 256 take 104 (the second launch walks 1024 chunks in one workgroup). Until
 // the last launch overwrites it, a chunk's own part of `pos` holds its counts.
 constexpr int kLayoutChunk = 1024;
 static_assert(kLayoutChunk >= kMaxExperts, "a chunk's counts fit in its part of pos");
@@ -877,7 +879,7 @@ __device__ __forceinline__ v4i pack8(const float (&v)[8]) {
 }
 
 // Rows past the Infinity Cache's size are read and written past the caches (kStream): 4096 tokens x 8
-// choices of 7168 (470 MB) forward 97 against 110 us, backward 190 against 204 us (5.3 TB/s; a plain copy
+// choices of 7168 (470 MB) forward 96 against 110 us, backward 188 against 204 us (5.3 TB/s; a plain copy
 // runs at 5.1). Smaller ones are still there from the kernel that wrote them: 512 tokens, forward 12.7 us
 // against 14.7 streamed, backward 24 against 30.
 // out[t] = sum_j w[t,j] y[pos[t,j]], summed in fp32 in the order of the choices and rounded once.

@@ -21,8 +21,8 @@ namespace {
 // maxima of a channel meet in LDS, and the codes leave through LDS as runs of 128 rows of one
 // channel (16-byte chunks XOR-swizzled by the channel's run of 8, which spreads the banks). Rows that
 // hold no token (row_pair < 0) and rows past the input are zero; blocks past the rows in use are left
-// alone. Bound by HBM: 2 or 4 bytes in, one out per element. 8192 rows of 7168 in bf16: 33 us, 5.4 TB/s;
-// 4001 of 18432: 38 us, 5.8 TB/s.
+// alone. Bound by HBM: 2 or 4 bytes in, one out per element. In a call on 9088 rows of 7168 in bf16: 46 us,
+// on 4001 of 18432: 53 us, 4.2 TB/s.
 template <bool kBf16, bool kPow2>
 __global__ __launch_bounds__(256) void cast_per_channel_kernel(ChannelCastProblem p, int64_t wg0) {
   __shared__ __attribute__((aligned(16))) float wave_amax[4][64], scale[64], reciprocal[64];
@@ -124,7 +124,8 @@ __device__ __forceinline__ int group_block(const WgradProblem& p, int i) {
 // registers; strips are read one (fp32) or two ahead of their MFMAs. Once the last strip is in registers
 // the stage is free: its refill goes out one load to an MFMA over the strips left, as the loads of
 // all waves at once keep the load path, and so the MFMAs behind them, busy for some 1000 cycles of a
-// block's 3500 (dense 4096 x 7168 x 18432: 446 -> 421 us with power-of-two scales, 554 -> 528 with fp32).
+// block's 3500 (bf16 results, 4096 x 7168 x 18432: 446 -> 421 us with power-of-two scales, 554 -> 528 with
+// fp32, in a row of products alone).
 //   kFp8 (bf16 results, fp32 scales): each MFMA starts from zero and its result is folded in with
 //   acc = fma(P, sk * sn, acc): a product and an FMA per element and block, one strip behind the MFMAs.
 //   kFp8Pow2 (bf16 results, power-of-two scales): the matrix unit applies them (lane l: row l & 15 of the
@@ -138,10 +139,12 @@ __device__ __forceinline__ int group_block(const WgradProblem& p, int i) {
 // workgroups are therefore persistent: each takes tiles slot, slot + grid, ..., and its loads run
 // ahead from one tile into the next, so that the next tile's first blocks arrive while this one's
 // results are written.
-// Measured: 8 experts of 1024 rows, 7168 x 2048, power-of-two scales 135 us (1.8 PFLOP/s; 235 MB of
-// results); 32 of 256 rows, 4096 x 2048, added to c 276 us (4.2 TB/s: bound by c and d); one matrix of 4001
-// rows, 7168 x 18432 528 us (2.0 PFLOP/s) and 421 us (2.5) with power-of-two scales, where the same
-// instructions on zeros take 357: the chip lowers its clock under the operands' switching.
+// Measured behind their casts, fp32 results: 8 experts of 1024 rows, 7168 x 2048, 332 us (470 MB of results);
+// 32 of 256 rows, 4096 x 2048, added to c 588 us (4.5 TB/s: bound by c and d); one matrix of 4001 rows, 7168 x
+// 18432, 1067 us (1.0 PFLOP/s; vector ALU 59 %, MFMA 44 % busy: two conversions and two operations of the fold
+// to an MFMA). bf16 results: 137 us with power-of-two scales (1.8 PFLOP/s); 280 us; 564 us (1.9 PFLOP/s) and 443
+// (2.4) with power-of-two scales, where the same instructions on zeros take a sixth less: the chip lowers its
+// clock under the operands' switching.
 // Two fp32 values as two bf16, round to nearest even (one instruction on gfx950).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -665,11 +668,11 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 }
 
 // Parts that a group's blocks are split into where the 128 x 128 tiles do not fill the chip. A block of a
-// tile takes about 0.75 us; a part writes its sums in fp32 and the join reads them, at about 3 TB/s, and
+// tile takes about 0.75 us (FP8 products; widened ones 1.2); a part writes its sums in fp32 and the join reads them, at about 3 TB/s, and
 // the join's launch costs some 4 us: the number of parts that makes the sum of these least, if that
-// is a tenth less than no parts. Measured, parts against none: 256 x 256 over 8192 rows 15.1 against 48.8 us,
-// 1024 x 1024 26.8 against 49.9, 512 x 512 over 2048 rows 12.6 against 15.5; no parts are taken for
-// 1024 x 1024 over 2048 rows (16.1 us; 4 parts 20.2).
+// is a tenth less than no parts. Measured, parts against none, fp32 (bf16) results: 256 x 256 over 8192 rows 17.1
+// against 76.6 us (15.1, 47.7), 1024 x 1024 33.3 against 78.0 (25.3, 48.3), 512 x 512 over 2048 rows 14.6 against
+// 23.2 (12.6, 15.3); no parts are taken for 1024 x 1024 over 2048 rows (23.7 us; bf16 15.5, and 20.2 in 4 parts).
 int wgrad_splits(int64_t G, int64_t M, int64_t N, int64_t K) {
   if (G < 1) return 1;
   const int64_t slots = 2 * (int64_t)cu_count(), tiles = (N / 128) * (K / 128) * G, blocks = M / kQ / G;
